@@ -73,6 +73,17 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
   return ok != 0;
 }
 
+// One arrival of the warp, once every lane's shared-memory loads have returned:
+// `word` is formed from a word of each of them (and may be anything).  What a
+// bulk copy refills is handed back this way: an arrival alone does not wait for
+// shared-memory loads still queued, and a refill did overtake them.
+__device__ __forceinline__ void mbar_arrive_behind_loads(uint64_t* bar, uint32_t word, bool ok) {
+  const uint32_t voted = __ballot_sync(0xFFFFFFFFu, word != 0u);
+  const uint32_t leader = voted ? __ffs(voted) - 1 : 0;
+  __syncwarp();
+  if (ok && (threadIdx.x & 31u) == leader) mbar_arrive(bar);
+}
+
 // Wait for the phase with the given parity to complete.  Gives up (returns
 // false) when `abort_flag` becomes nonzero or after `limit_ns`; in the latter
 // case it sets `*abort_flag` and reports kStatusTimeout.

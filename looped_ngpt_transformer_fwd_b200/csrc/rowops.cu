@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) row_update_kernel(const 
 // ...) through a ring of shared-memory stages that one producer lane fills
 // with bulk copies (y, h, and e when re-injecting: one d-float vector each),
 // so loads stay in flight while the eight consumer warps reduce.  A consumer
-// warp frees a stage as soon as its values are in registers.  Consumer
+// warp frees a stage once its values are in registers.  Consumer
 // thread t holds the same chunks as thread t of row_update_kernel and the
 // block sums add the same warp sums in the same order: the results are
 // bit-identical to that kernel's.
@@ -298,6 +298,7 @@ __global__ void __launch_bounds__(kPipeThreads, 2)
     const float4* se = sh + nch;
     float4 y[kPipeChunks], h[kPipeChunks], e[kPipeChunks];
     float ss = 0.f;
+    uint32_t read = 0u;                          // a word of every load
 #pragma unroll
     for (int j = 0; j < kPipeChunks; ++j) {
       const int c = t + j * kPipeConsumers;
@@ -308,9 +309,9 @@ __global__ void __launch_bounds__(kPipeThreads, 2)
         if (reinject) e[j] = se[c];
         ss += dot4(y[j], y[j]);
       }
+      read ^= __float_as_uint(y[j].x) ^ __float_as_uint(h[j].x) ^ __float_as_uint(e[j].x);
     }
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&empty[s]);       // the stage may take a later row
+    mbar_arrive_behind_loads(&empty[s], read, ok);   // the stage may take a later row
     // a consumer warp whose wait gave up makes every consumer stop here
     const float2 s1 = consumer_sum2(ss, ok ? 0.f : 1.f, red, nred);
     if (s1.y > 0.f) break;

@@ -412,18 +412,12 @@ __device__ __forceinline__ void load_stage(float4 (&x)[kPer], const float* src, 
                  : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
   }
 }
-// Hand a stage back to the producer once every lane's loads from it have
-// returned: an arrival does not wait for shared-memory loads still queued, and
-// with 24 warps loading at once a refill did overtake them.  The vote needs a
-// word of each load.
+// Hand a stage back to the producer once it has been read.
 __device__ __forceinline__ void free_stage(const float4 (&x)[kPer], uint64_t* empty, bool ok) {
   uint32_t w = 0u;
 #pragma unroll
   for (int j = 0; j < kPer; ++j) w ^= __float_as_uint(x[j].x) ^ __float_as_uint(x[j].w);
-  const uint32_t voted = __ballot_sync(kFull, w != 0u);
-  const int lane = threadIdx.x & 31, leader = voted ? __ffs(voted) - 1 : 0;
-  __syncwarp();
-  if (ok && lane == leader) mbar_arrive(empty);
+  mbar_arrive_behind_loads(empty, w, ok);
 }
 template <bool kNear>
 __device__ __forceinline__ void exp_stage(float4 (&x)[kPer], float c, const ExpBase& b) {
