@@ -61,14 +61,16 @@ class KVCache:
             pass
 
 
-def _table(v, dtype, device):
-    """A vocabulary table on the device: numpy (bf16 as uint16 bits) or torch."""
-    if isinstance(v, torch.Tensor):
-        if v.dtype != dtype:
-            raise ValueError(f"vocabulary table of {v.dtype}: {dtype} is wanted")
-        return v.to(device).contiguous()
-    a = np.ascontiguousarray(v)
-    return torch.from_numpy(a.view(np.int16) if a.dtype == np.uint16 else a).to(device)
+def _table(name, v, dtype, device):
+    """A vocabulary table on the device: numpy or torch, bf16 values as such or as
+    their bits (uint16 / int16)."""
+    kinds = (dtype,) if dtype == torch.float32 else (dtype, torch.uint16, torch.int16)
+    if not isinstance(v, torch.Tensor):
+        a = np.ascontiguousarray(v)
+        v = torch.from_numpy(a.view(np.int16) if a.dtype == np.uint16 else a)
+    elif v.dtype not in kinds:
+        raise ValueError(f"{name}: a table of {v.dtype}: {dtype} is wanted")
+    return v.to(device).contiguous()
 
 
 def _expect(name, t, shape, dtype, device):
@@ -99,8 +101,9 @@ def _stream_of(stream, device):
 
 
 class Vocab:
-    """Embedding and output tables bound to a model (dory_vocab_create).  The
-    tables are numpy arrays (bf16 as uint16 bits) or torch tensors."""
+    """Embedding and output tables bound to a model (dory_vocab_create): emb_in and
+    emb_out [V, d] (torch.bfloat16, or the bits as uint16 / int16, numpy or torch)
+    and logit_scale [V] (float32)."""
 
     def __init__(self, model, tables):
         self.model = model
@@ -109,8 +112,8 @@ class Vocab:
         if self.nbytes == 0:
             raise ValueError("vocabulary size must be a positive multiple of 256")
         self.buf = torch.empty(self.nbytes, dtype=torch.uint8, device=model.device)
-        staged = {k: _table(v, torch.float32 if k == "logit_scale" else torch.bfloat16, model.device)
-                  for k, v in tables.items()}
+        staged = {k: _table(k, tables[k], dtype, model.device) for k, dtype in (
+            ("emb_in", torch.bfloat16), ("emb_out", torch.bfloat16), ("logit_scale", torch.float32))}
         self.handle = B.dory_vocab_create(model.handle, self.size, _ptr(staged["emb_in"]),
                                           _ptr(staged["emb_out"]), _ptr(staged["logit_scale"]),
                                           _ptr(self.buf), self.nbytes, _stream(None))
