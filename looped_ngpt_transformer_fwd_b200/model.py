@@ -6,6 +6,7 @@ KV caches, workspaces) as torch tensors and forwards every call to the C ABI
 """
 
 import ctypes
+import math
 
 import numpy as np
 import torch
@@ -61,15 +62,19 @@ class KVCache:
             pass
 
 
-def _table(name, v, dtype, device):
+def _table(name, v, shape, dtype, device):
     """A vocabulary table on the device: numpy or torch, bf16 values as such or as
-    their bits (uint16 / int16)."""
+    their bits (uint16 / int16).  A leading axis of V rows, or all values flat."""
     kinds = (dtype,) if dtype == torch.float32 else (dtype, torch.uint16, torch.int16)
     if not isinstance(v, torch.Tensor):
         a = np.ascontiguousarray(v)
+        if a.dtype not in (np.float32, np.uint16, np.int16):
+            raise ValueError(f"{name}: a table of {a.dtype}: {dtype} is wanted")
         v = torch.from_numpy(a.view(np.int16) if a.dtype == np.uint16 else a)
-    elif v.dtype not in kinds:
+    if v.dtype not in kinds:
         raise ValueError(f"{name}: a table of {v.dtype}: {dtype} is wanted")
+    if v.numel() != math.prod(shape) or v.shape[0] not in (shape[0], v.numel()):
+        raise ValueError(f"{name}: a table {list(shape)} is wanted, not {list(v.shape)}")
     return v.to(device).contiguous()
 
 
@@ -112,8 +117,10 @@ class Vocab:
         if self.nbytes == 0:
             raise ValueError("vocabulary size must be a positive multiple of 256")
         self.buf = torch.empty(self.nbytes, dtype=torch.uint8, device=model.device)
-        staged = {k: _table(k, tables[k], dtype, model.device) for k, dtype in (
-            ("emb_in", torch.bfloat16), ("emb_out", torch.bfloat16), ("logit_scale", torch.float32))}
+        rows, d = self.size, model.cfg["d_model"]
+        staged = {k: _table(k, tables[k], shape, dtype, model.device) for k, shape, dtype in (
+            ("emb_in", (rows, d), torch.bfloat16), ("emb_out", (rows, d), torch.bfloat16),
+            ("logit_scale", (rows,), torch.float32))}
         self.handle = B.dory_vocab_create(model.handle, self.size, _ptr(staged["emb_in"]),
                                           _ptr(staged["emb_out"]), _ptr(staged["logit_scale"]),
                                           _ptr(self.buf), self.nbytes, _stream(None))

@@ -54,3 +54,17 @@ def test_tables_in_every_form(create, form):
 
 def test_other_entries_are_not_looked_at(create):
     assert create(name="tables", extra=np.zeros(3)) == [BITS.tobytes(), BITS.tobytes(), SCALE.tobytes()]
+
+
+@pytest.mark.parametrize("kw", [
+    dict(emb_in=BITS[:-1]), dict(emb_out=BITS[:, :-2]), dict(emb_in=np.ascontiguousarray(BITS.T)),
+    dict(emb_out=BITS.reshape(V // 2, 2 * D)), dict(emb_in=TORCH_BITS[: V // 2]),
+    dict(emb_in=np.zeros((V, D), np.float32)), dict(emb_out=np.zeros((V, D), np.float16)),
+    dict(emb_in=torch.zeros(V, D)), dict(emb_out=torch.zeros(V, D, dtype=torch.float16)),
+    dict(emb_in=np.zeros((V, D), np.int64)), dict(logit_scale=SCALE.astype(np.float64)),
+    dict(logit_scale=torch.ones(V, dtype=torch.bfloat16)), dict(logit_scale=np.ones(V, np.uint16)),
+    dict(logit_scale=np.ones((V, 2), np.float32)), dict(emb_in=np.zeros((V, D // 2), np.float32)),
+])
+def test_refused_tables(create, kw):
+    with pytest.raises(ValueError):
+        create(**kw)
