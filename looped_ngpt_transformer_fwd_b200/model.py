@@ -276,6 +276,8 @@ class DoryModel:
                  weight_format="bf16"):
         self.cfg = cfg
         self.device = torch.device(device)
+        if self.device.type != "cuda":
+            raise ValueError(f"device = {device}: a CUDA device is wanted")
         if self.device.index is None:
             self.device = torch.device("cuda", torch.cuda.current_device())
         self.weight_format = weight_format

@@ -1,4 +1,5 @@
-"""The forms in which the vocabulary's tables are taken, on a host without a GPU."""
+"""The forms in which the vocabulary's tables are taken and the devices a model takes,
+on a host without a GPU."""
 
 import ctypes
 
@@ -68,3 +69,11 @@ def test_other_entries_are_not_looked_at(create):
 def test_refused_tables(create, kw):
     with pytest.raises(ValueError):
         create(**kw)
+
+
+@pytest.mark.parametrize("device", ["cpu", torch.device("cpu"), "meta"])
+def test_a_model_is_on_a_cuda_device(device):
+    from looped_ngpt_transformer_fwd_b200.model import DoryModel
+    from synthetic import load_config
+    with pytest.raises(ValueError):
+        DoryModel(load_config("tiny"), lambda b: pytest.fail("weights were asked for"), device=device)
