@@ -172,7 +172,7 @@ __device__ __forceinline__ ExpSum load_entries(Entries& x, const DistillParams& 
     if (q * 32 >= p.k) break;
     sum.s += exp_term(x.t[q], c, ref);
   }
-  sum = warp_join(sum, c);
+  sum = softmax_sum(warp_join(sum, c));
 #pragma unroll
   for (int q = 0; q < kOwn; ++q) {
     if (q * 32 >= p.k) break;
@@ -243,7 +243,7 @@ __global__ void __launch_bounds__(kRowThreads + 32, 2) distill_row_kernel(const 
     clear_slots(sh.slot, lane, 32);
   }
   __syncthreads();
-  const ExpSum acc = warp_join(lane < warps ? sh.sums[lane] : ExpSum{-INFINITY, 0.f}, c);
+  const ExpSum acc = softmax_sum(warp_join(lane < warps ? sh.sums[lane] : ExpSum{-INFINITY, 0.f}, c));
   const bool empty = acc.s == 0.f || sh.teacher.s == 0.f;
   const float inv = empty ? 0.f : p.grad_scale * w / acc.s;
   if (warp < warps && dz) {
@@ -604,7 +604,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) distill_ring_kernel(const Dis
       if (lane == 0) sh.part[used & 1][warp] = acc;
       ok = ok && __all_sync(kFull, mbar_wait_bounded(&sh.tfull[b], used / kTeachers & 1, abort_flag, p.status));
       consumer_sync();
-      acc = warp_join(lane < kConsumerWarps ? sh.part[used & 1][lane] : ExpSum{-INFINITY, 0.f}, c);
+      acc = softmax_sum(warp_join(lane < kConsumerWarps ? sh.part[used & 1][lane] : ExpSum{-INFINITY, 0.f}, c));
       if (tid == 0) sh.teacher[b].student = acc;
       ++used;
       if (dz) {

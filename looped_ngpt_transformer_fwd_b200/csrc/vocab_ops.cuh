@@ -22,13 +22,18 @@ __device__ __forceinline__ float warp_max(float v) {
 // so far, m their maximum.  x - m is formed first: it is exact next to the
 // maximum, and further off its rounding is relative to the difference, whereas
 // a rounded c m would scale the whole sum by up to an ulp of |c m|.
-// Empty, or every value -inf: m = -inf, s = 0.  A NaN value makes s NaN, and so
-// does +inf (m = +inf).
+// Empty, or every value -inf: m = -inf, s = 0.  A NaN value makes s NaN;
+// without one, +inf makes it +inf (m = +inf).
 struct ExpSum {
   float m, s;
 };
-// what to subtract in exponents: the maximum, or 0 while there is none
-__device__ __forceinline__ float exp_ref(float m) { return m == -INFINITY ? 0.f : m; }
+// what to subtract in exponents: the maximum, 0 while there is none, and a finite
+// value below +inf, so that only a NaN gives NaN
+__device__ __forceinline__ float exp_ref(float m) {
+  return m == -INFINITY ? 0.f : fminf(m, 3.402823466e38f);
+}
+// a softmax's sum: infinite values have no shares, NaN
+__device__ __forceinline__ ExpSum softmax_sum(ExpSum a) { return {a.m, a.m == INFINITY ? NAN : a.s}; }
 
 __device__ __forceinline__ float exp_term(float x, float c, float ref) {
   return exp2_fast((x - ref) * c);

@@ -32,9 +32,8 @@ constexpr float kLog2e = 1.4426950408889634f;
 // log of a sum of exponentials; log2 s over the fp32 constant that scaled the
 // differences, so that its rounding (nearly) cancels
 __device__ __forceinline__ float log_of(const ExpSum& a) {
-  return a.m == INFINITY ? INFINITY
-                         : static_cast<float>(static_cast<double>(exp_ref(a.m)) +
-                                              static_cast<double>(log2f(a.s)) / static_cast<double>(kLog2e));
+  return static_cast<float>(static_cast<double>(exp_ref(a.m)) +
+                            static_cast<double>(log2f(a.s)) / static_cast<double>(kLog2e));
 }
 
 // A candidate: its key, then the lower token first.
