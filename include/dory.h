@@ -355,7 +355,8 @@ DORY_API int dory_distill(dory_vocab* v, const float* logits, int n, const int32
 
 /* Gradient of dory_embed: d_emb [vocab, d_model] (fp32) from the tokens and
  * dL/dh [n, d_model] (fp32, device) of the rows it returned.  For each token t,
- * G = sum of its rows of dh (in a fixed order: the same bits every time) and
+ * G = sum of its rows of dh (in a fixed order, the same bits every time: up to 64
+ * rows in a row in fp32, what goes beyond joined in fp64) and
  *   d_emb[t] = (G - e (e . G) / |e|^2) / |e|,  e = emb_in[t]
  * (|e|^2 below 1e-20, where the lookup clamps the norm: 1e10 G).  accumulate =
  * 0 overwrites all of d_emb (zero where no token points), nonzero adds to the

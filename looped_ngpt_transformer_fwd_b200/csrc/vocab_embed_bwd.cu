@@ -7,7 +7,9 @@
 // The tokens are sorted by (token, row), so equal tokens lie together; windows of
 // the sorted list are summed independently, each finishing the runs that start
 // in it, except that a long run is summed window by window and joined by a
-// second kernel.  Every sum has a fixed order.
+// second kernel.  Every sum has a fixed order: at most 64 rows one after the other
+// in 32 bits, the windows of a longer run in 64, rounded to 32 before the
+// projection.
 //
 // Bound: HBM where the table is written: 32768 rows of 2048 into 131072 x 2048
 // (tokens by frequency) 249 us, floor 212.  Adding to few rows is bound by the
@@ -450,13 +452,22 @@ __global__ void __launch_bounds__(256, NV == 1 ? (Add ? 3 : 4) : NV == 2 ? 4 : 2
 }
 
 // The long runs: 64 columns of one run's pieces a time, 16 threads across and 16
-// down; the CTA that completes the run's last columns finishes the row.
+// down; the CTA that completes the run's last columns finishes the row.  The
+// pieces are joined in 64 bits: a run may have n / 32 of them, and a chain of so
+// many additions in 32 bits can drift by more than a window's sum ever does.
 constexpr int kJoinThreads = 256;
 constexpr int kJoinCols = 64;
 
+struct Sum4 {
+  double x = 0.0, y = 0.0, z = 0.0, w = 0.0;
+  __device__ __forceinline__ void add(const float4 b) {
+    x += b.x; y += b.y; z += b.z; w += b.w;
+  }
+};
+
 template <int NV>
 __global__ void __launch_bounds__(kJoinThreads) long_run_kernel(const RunSumParams p) {
-  __shared__ float4 sums[16][16];
+  __shared__ double sums[16][4][16];
   __shared__ float2 part[8];
   __shared__ int n_pieces, last;
   wait_for_previous();
@@ -475,7 +486,7 @@ __global__ void __launch_bounds__(kJoinThreads) long_run_kernel(const RunSumPara
     const int n = n_pieces;
     const float4* pieces = reinterpret_cast<const float4*>(p.pieces);
     const size_t cols = p.d / 4;
-    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    Sum4 s;
     for (int k0 = y; k0 < n; k0 += 64) {
       float4 v[4];
 #pragma unroll
@@ -485,13 +496,17 @@ __global__ void __launch_bounds__(kJoinThreads) long_run_kernel(const RunSumPara
         if (k < n) v[q] = pieces[(2 * static_cast<size_t>(w + k) + (k == 0)) * cols + col];
       }
 #pragma unroll
-      for (int q = 0; q < 4; ++q) add4(s, v[q]);
+      for (int q = 0; q < 4; ++q) s.add(v[q]);
     }
-    sums[y][x] = s;
+    sums[y][0][x] = s.x;
+    sums[y][1][x] = s.y;
+    sums[y][2][x] = s.z;
+    sums[y][3][x] = s.w;
     __syncthreads();
-    if (y == 0) {
-      for (int k = 1; k < 16; ++k) add4(s, sums[k][x]);
-      reinterpret_cast<float4*>(p.long_sums)[static_cast<size_t>(run) * cols + col] = s;
+    if (y < 4) {   // a thread per column
+      double sum = 0.0;
+      for (int k = 0; k < 16; ++k) sum += sums[k][y][x];
+      p.long_sums[static_cast<size_t>(run) * p.d + col * 4 + y] = static_cast<float>(sum);
       __threadfence();
     }
     __syncthreads();
