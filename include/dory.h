@@ -363,8 +363,9 @@ DORY_API int dory_distill(dory_vocab* v, const float* logits, int n, const int32
  * rows of the tokens present and touches no other.  A token outside
  * 0..vocab-1 counts for nothing and gives DORY_ERR_DEVICE_BOUNDS from
  * dory_device_status.  n at most 2^24; `ws` of
- * dory_embed_backward_workspace_bytes, 256-byte aligned, any contents.  Calls
- * that may overlap on the GPU need a workspace (and a d_emb) each. */
+ * dory_embed_backward_workspace_bytes, 256-byte aligned, any contents.  d_emb
+ * and `ws` overlap neither each other nor an input.  Calls that may overlap on
+ * the GPU need a workspace (and a d_emb) each. */
 DORY_API size_t dory_embed_backward_workspace_bytes(const dory_vocab* v, int n);
 DORY_API int dory_embed_backward(dory_vocab* v, const int32_t* d_tokens, int n, const float* dh,
                                  float* d_emb, int accumulate, void* ws, size_t ws_bytes,

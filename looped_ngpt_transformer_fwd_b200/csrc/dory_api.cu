@@ -2287,7 +2287,14 @@ int dory_embed_backward(dory_vocab* v, const int32_t* d_tokens, int n, const flo
     return DORY_ERR_INVALID_ARG;
   if (!is_aligned(ws) || !is_aligned(dh, 16) || !is_aligned(d_emb, 16) || !is_aligned(d_tokens, 4))
     return DORY_ERR_MISALIGNED;
-  if (ws_bytes < embed_bwd_workspace_bytes(n, v->m->d, v->m->num_sms)) return DORY_ERR_BUFFER_TOO_SMALL;
+  const size_t ws_need = embed_bwd_workspace_bytes(n, v->m->d, v->m->num_sms);
+  if (ws_bytes < ws_need) return DORY_ERR_BUFFER_TOO_SMALL;
+  // rows of the table and of the workspace are written while inputs are still read
+  const size_t row = size_t(v->m->d) * 4, table = v->vocab * row;
+  if (overlap(d_emb, table, dh, n * row) || overlap(d_emb, table, d_tokens, size_t(n) * 4) ||
+      overlap(d_emb, table, ws, ws_need) || overlap(ws, ws_need, dh, n * row) ||
+      overlap(ws, ws_need, d_tokens, size_t(n) * 4))
+    return DORY_ERR_INVALID_ARG;
   if (!vocab_device(v)) return DORY_ERR_INVALID_ARG;
   if (launch_embed_bwd(v->emb_in, v->vocab, v->m->d, d_tokens, n, dh, d_emb, accumulate, ws,
                        v->m->num_sms, v->m->status, static_cast<cudaStream_t>(stream)) != cudaSuccess)

@@ -1,4 +1,5 @@
-"""The embedding gradient of many rows: long runs of one token."""
+"""The embedding gradient of many rows, long runs of one token, and buffers that
+overlap."""
 
 import numpy as np
 import pytest
@@ -82,3 +83,28 @@ def test_many_rows_of_nonzero_mean(n, kind, accumulate):
     again = voc.embed_backward(tok, dh, out=was.clone(), accumulate=accumulate)
     assert torch.equal(again, got)
     assert model.device_status() == 0
+
+
+def test_overlapping_buffers_are_refused():
+    """The table's gradient in the place of an input or of the workspace, whole or in part."""
+    from looped_ngpt_transformer_fwd_b200 import binding as B
+    V, d, n = 256, 128, 256
+    model, voc = make_vocab(V, d)
+    row = d * 4
+    need = B.dory_embed_backward_workspace_bytes(voc.handle, n)
+    buf = torch.zeros(2 * V * row + n * row + n * 4 + 2 * need + 1024, dtype=torch.uint8, device="cuda")
+    p = (buf.data_ptr() + 255) // 256 * 256
+    table, dh, tok, ws = p, p + V * row, p + V * row + n * row, p + V * row + n * row + n * 4
+
+    def call(tok=tok, dh=dh, table=table, ws=ws, size=need):
+        return B.lib().dory_embed_backward(voc.handle, tok, n, dh, table, 0, ws, size, None)
+    assert call(dh=table) == -1 and call(dh=table + V * row - 16) == -1 and call(table=dh + 16) == -1
+    assert call(tok=table + 4) == -1 and call(tok=ws) == -1 and call(dh=ws) == -1
+    assert call(ws=table) == -1 and call(ws=dh + n * row - 256) == -1 and call(ws=tok - 256) == -1
+    torch.cuda.synchronize()
+    assert not buf.any()
+    assert call() == 0 and model.device_status() == 0      # neighbours, none overlapping
+    dh = torch.ones(n, d, device="cuda")
+    with pytest.raises(B.DoryError):
+        voc.embed_backward(torch.zeros(n, dtype=torch.int32, device="cuda"), dh, out=dh)
+    assert (dh == 1).all()
