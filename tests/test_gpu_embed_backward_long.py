@@ -85,6 +85,28 @@ def test_many_rows_of_nonzero_mean(n, kind, accumulate):
     assert model.device_status() == 0
 
 
+@pytest.mark.parametrize("n", [8200, 262150])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_tokens_of_three_sort_passes(n, accumulate):
+    """A vocabulary of 2^18 tokens: 19 bits of key, three passes."""
+    V, d = 1 << 18, 128
+    g = torch.Generator(device="cuda").manual_seed(n)
+    E = torch.randn(V, d, device="cuda", generator=g).bfloat16()
+    model, voc = make_vocab(V, d, emb=E)
+    tok = (V * torch.rand(n, device="cuda", generator=g) ** 3).int()
+    tok[::7], tok[1::50], tok[-1] = 4099, V - 1, 0
+    dh = torch.randn(n, d, device="cuda", generator=g)
+    was = torch.randn(V, d, device="cuda", generator=g)
+    got = voc.embed_backward(tok, dh, out=was.clone(), accumulate=accumulate)
+    was = was if accumulate else torch.zeros_like(was)
+    ref = reference(E, tok, dh, was)
+    assert ((got.double() - ref).abs() - bound(E, tok, dh, ref, was)).max() <= 0
+    absent = torch.ones(V, dtype=torch.bool, device="cuda")
+    absent[tok.long()] = False
+    assert torch.equal(got[absent], was[absent])
+    assert model.device_status() == 0
+
+
 def test_overlapping_buffers_are_refused():
     """The table's gradient in the place of an input or of the workspace, whole or in part."""
     from looped_ngpt_transformer_fwd_b200 import binding as B

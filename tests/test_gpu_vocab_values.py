@@ -1,4 +1,6 @@
-"""Infinities and NaN in the operators around the vocabulary, in every kernel form."""
+"""Values and sizes of the operators around the vocabulary in every kernel form:
+infinities and NaN, and more answers than groups of logits.
+"""
 
 import math
 
@@ -6,7 +8,8 @@ import numpy as np
 import pytest
 import torch
 
-from tests.test_gpu_vocab_ops import cuda, distill_bounds, distill_case, make_vocab, OV
+from tests.test_gpu_vocab_ops import (OV, cuda, distill_bounds, distill_case, lse_bound, make_vocab,
+                                      top_rows)
 
 pytestmark = pytest.mark.gpu
 
@@ -49,4 +52,45 @@ def test_distill_of_infinite_logits(V):
     for i in (0, 3):
         assert abs(float(loss[i]) - rl[i]) <= bl[i]
         assert np.all(np.abs(dz[i].double().cpu().numpy() - rz[i]) <= bz[i])
+    assert model.device_status() == 0
+
+
+@pytest.mark.parametrize("n,V", FORMS)
+def test_top_of_rows_with_fewer_numbers_than_answers(n, V):
+    """Answers that reach into the NaNs: by ascending token, wherever they stand
+    (scattered, whole groups, all but a few)."""
+    model, voc = make_vocab(V)
+    rng = np.random.default_rng(V + 1)
+    for k in (5, 70, 256):
+        z = np.full((n, V), np.nan, np.float32)
+        z[0, rng.permutation(V)[: k // 2]] = rng.standard_normal(k // 2)
+        z[-1, :k // 2] = -np.inf
+        if n > 2:
+            z[1] = rng.standard_normal(V)
+            z[1, rng.random(V) < 0.9] = np.nan
+            z[1, V // 2:] = np.nan
+        values, tokens, lse = voc.top(cuda(z), k)
+        rv, rt, _ = OV.top_logits(z, k)
+        assert np.array_equal(tokens.cpu().numpy(), rt), k
+        assert np.array_equal(values.double().cpu().numpy(), rv, equal_nan=True)
+        assert torch.isnan(lse).all()
+    assert model.device_status() == 0
+
+
+@pytest.mark.parametrize("n,V,k", [(3, 2304, 256), (3, 4096, 200), (200, 4096, 129), (3, 7936, 249)])
+@pytest.mark.parametrize("kind", ["plain", "ties", "equal", "none", "few", "up", "down", "cluster", "zeros",
+                                  "wide"])
+def test_top_with_more_answers_than_groups(n, V, k, kind):
+    """Rows of fewer groups of 32 logits than answers: every logit is a candidate."""
+    model, voc = make_vocab(V)
+    z = top_rows(kind, n, V, V + k)
+    values, tokens, lse = voc.top(cuda(z), k)
+    rv, rt, rl = OV.top_logits(z, k)
+    assert np.array_equal(tokens.cpu().numpy(), rt)
+    assert np.array_equal(values.double().cpu().numpy(), rv)
+    got = lse.double().cpu().numpy()
+    if kind == "none":
+        assert np.all(got == -np.inf)
+    else:
+        assert np.all(np.abs(got - rl) <= lse_bound(V, rl))
     assert model.device_status() == 0
