@@ -106,8 +106,8 @@ constexpr int kRowWarps = 4;    // per CTA
 constexpr int kByGroup = 64;    // 4 * kByGroup candidates fit the list
 
 // T: the highest threshold that at least k of the warp's keys reach, from the
-// highest bit down, or one that exactly k reach; returns how many do.  `all` keys
-// are there, the others are 0.
+// highest bit down, or one that exactly k reach; returns how many do.  `all` >= k
+// keys are there, the others are 0.
 template <int kN>
 __device__ __forceinline__ int warp_kth(const uint32_t (&key)[kN], uint32_t lo, int all, int k, uint32_t& T) {
   uint32_t hi = 0u;
@@ -115,8 +115,8 @@ __device__ __forceinline__ int warp_kth(const uint32_t (&key)[kN], uint32_t lo, 
   for (int i = 0; i < kN; ++i) hi = max(hi, key[i]);
   lo = __reduce_min_sync(kFull, lo);
   hi = __reduce_max_sync(kFull, hi);
-  T = all < k ? 0u : lo;
-  if (all <= k || lo == hi) return all;
+  T = lo;
+  if (all == k || lo == hi) return all;
   int bit = 31 - __clz(lo ^ hi), reach = all;
   T = hi >> bit >> 1 << 1 << bit;
   for (; bit >= 0 && reach != k; --bit) {
@@ -452,13 +452,12 @@ __global__ void __launch_bounds__(kT)
   if (n > kListMax) {
     // answers crowded into few groups: cut to the k largest words, which all
     // differ, bit by bit over the groups' logits (read again, from L1 or L2)
-    uint64_t bar = static_cast<uint64_t>(T) << 32;
     __syncthreads();
     if (tid < 4) slot[tid] = 0;
     if (tid == 0) n_list = 0;
     __syncthreads();
     int have = n;
-    bar = 0u;
+    uint64_t bar = 0u;
     for (int bit = 63, turn = 0; bit >= 0 && have != k; --bit, ++turn) {
       const uint64_t cand = bar | 1ull << bit;
       int c = 0;
