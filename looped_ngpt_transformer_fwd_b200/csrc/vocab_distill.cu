@@ -652,11 +652,15 @@ cudaError_t launch(const DistillParams& p, int num_sms, cudaStream_t s) {
     distill_row_kernel<Grad><<<p.n, threads, 0, s>>>(p);
     return cudaGetLastError();
   }
-  // bf16 gradient through the scale, 402 M logits (floor 370 us), turns taken or
-  // not: 12288 x 32768 477 and 497 us, 8192 x 49152 420 and 432, 6144 x 65536
-  // 440 and 453 (but fp32 628 and 536), 4096 x 98304 473 and 425, rows of 131072
-  // 524 and 450: with turns the rows in flight, one and a half per SM, outgrow L2.
-  return p.vocab > 49152 ? launch_ring<Grad, false>(p, num_sms, s) : launch_ring<Grad, true>(p, num_sms, s);
+  // 402 M logits, turns taken or not, in us.  bf16 gradient through the scale (floor
+  // 370): rows of 16640 710 and 696, 20480 600 and 603, 24576 483 and 565, 32768 489
+  // and 524, 49152 425 and 458, 65536 447 and 470, 98304 481 and 440, 131072 538 and
+  // 461: with turns the rows in flight, one and a half per SM, outgrow L2 in the end.
+  // fp32 (floor 492): 16640 759 and 684, 24576 580 and 505, 49152 601 and 536, 65536
+  // 648 and 545, 131072 707 and 632.
+  if constexpr (sizeof(Grad) == 2)
+    if (p.vocab <= 65536) return launch_ring<Grad, true>(p, num_sms, s);
+  return launch_ring<Grad, false>(p, num_sms, s);
 }
 
 }  // namespace
