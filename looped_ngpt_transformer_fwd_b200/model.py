@@ -181,6 +181,9 @@ class Vocab:
             _expect("bias_tokens", bias_tokens, (n, nb), i32, dev),
             _expect("bias_values", bias_values, (n, nb), f32, dev), nb,
             _expect("allowed", allowed, (n, self.size // 32), i32, dev))
+        if history is not None and ld == 0:   # nothing seen yet: no penalties
+            for part in ("history_len", "prompt_len", "repetition", "frequency", "presence"):
+                setattr(c, part, None)
         if out is None:
             out = _empty(z, (n, self.size), f32, stream)
         op = _expect("out", out, (n, self.size), f32, dev)
