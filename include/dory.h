@@ -285,13 +285,17 @@ DORY_API int dory_lm_head(dory_vocab* v, const void* h, int n, float* logits, vo
 DORY_API int dory_sample(dory_vocab* v, const float* logits, int n, float temperature,
                          uint32_t seed, const int32_t* d_steps, int32_t* d_tokens, void* stream);
 
+/* The operators around the vocabulary from here on want the model's device to be
+ * the current one (DORY_ERR_INVALID_ARG otherwise). */
+
 /* What dory_adjust_logits applies to a row; a NULL pointer leaves its part out.
  * All arrays are device arrays, read when the kernels run. */
 #define DORY_MAX_BIASES 1024
 typedef struct dory_logit_controls {
   const int32_t* history;     /* [n, history_ld] the row's tokens so far, prompt first; a
                                  negative entry is padding                               */
-  int32_t history_ld;
+  int32_t history_ld;         /* rows of more than 65534 entries take longer, whatever
+                                 is in use of them                                       */
   const int32_t* history_len; /* [n] entries of each row in use (with history)           */
   const int32_t* prompt_len;  /* [n] how many of them are the prompt; NULL = none        */
   const float* repetition;    /* [n] r > 0 (1 = off): every token of the history         */
@@ -311,9 +315,10 @@ typedef struct dory_logit_controls {
  *   z += biases of v;   out = allowed ? z : -inf.
  * The penalties need a history.  A token of history or biases at or above the
  * vocabulary size, or a history_len outside 0..history_ld (clamped), is
- * ignored and gives DORY_ERR_DEVICE_BOUNDS from dory_device_status.  A row
- * whose mask allows nothing becomes -inf throughout, for which dory_sample
- * writes the token 0x7fffffff (dory_embed reports it as out of range). */
+ * ignored and gives DORY_ERR_DEVICE_BOUNDS from dory_device_status; a prompt_len
+ * is clamped to 0..history_len.  A row whose mask allows nothing becomes -inf
+ * throughout, for which dory_sample writes the token 0x7fffffff (dory_embed
+ * reports it as out of range). */
 DORY_API int dory_adjust_logits(dory_vocab* v, const float* logits, int n,
                                 const dory_logit_controls* controls, float* out, void* stream);
 
@@ -334,7 +339,9 @@ typedef enum dory_grad_format { DORY_GRAD_F32 = 0, DORY_GRAD_BF16 = 1 } dory_gra
  * checkpoints are distilled from the BF16 teacher; the page gives no formula,
  * this is the usual one).  Row i has k (1..DORY_MAX_TOP) entries
  * teacher_tokens / teacher_logits [n, k] (a negative token is an unused entry;
- * entries of one token add up).  With T = temperature (1e-3..1e3),
+ * entries of one token add up in the gradient; the loss is the sum over entries
+ * all the same, which differs from the divergence with their shares added up by a
+ * term without logits).  With T = temperature (1e-3..1e3),
  *   p = softmax(teacher_logits / T) over the row's entries,
  *   q = softmax(logits / T) over the vocabulary, w = row_weight[i] (NULL = 1),
  *   loss[i] = w T^2 sum_j p_j (log p_j - log q_j),

@@ -249,6 +249,11 @@ cudaError_t launch_adjust(AdjustParams p, int num_sms, cudaStream_t s) {
   // The largest chunk that still gives every SM one (fewer re-reads of the
   // history), but none that a whole row does not half fill.  64 rows x 131072
   // with 4096 tokens of history: chunks of 32768 13 us, of 8192 17 us.
+  // Cells go by the width of the history's rows, as their lengths are on the
+  // device: rows wider than kMaxShort pay for 32-bit cells and chunks of 8192 with
+  // few tokens too.  256 rows x 131072 with up to 1000 / 4096 / 32768 / 65534
+  // tokens in rows of at most 65534 entries take 62 / 65 / 75 / 92 us, in wider
+  // ones 68 / 76 / 103 / 142; 64 rows with up to 4096 21-23 and 25; one row 10 and 12.
   auto fits = [&](int chunk) {
     return p.vocab > chunk / 2 && static_cast<long long>(p.n) * ((p.vocab + chunk - 1) / chunk) >= num_sms;
   };

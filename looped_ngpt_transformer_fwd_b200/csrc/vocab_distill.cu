@@ -17,7 +17,9 @@
 // 16384 304 (247), 32768 x 4096 169 (126), 65536 x 1024 128 (67).  The loss alone
 // of 3000 x 131072 231 (241: reads alone run above the copy rate).  Two CTAs of a cluster with half a row each, in
 // registers or in a ring, were slower: their rows run in step, and memory waits
-// while they join their sums.
+// while they join their sums.  Two CTAs of 544 threads leave the row kernel 56
+// registers and 896 threads the ring 72; what does not fit goes to local memory
+// (48-56 bytes a thread in the row kernel, 16-24 in the ring).
 #include "kernels.h"
 #include "vocab_ops.cuh"
 

@@ -15,7 +15,7 @@
 // (tokens by frequency) 249 us, floor 212.  Adding to few rows is bound by the
 // chain of launches: 4096 rows into the same table 29 us (floor 12), the sort 8,
 // the sums 20 and the joining of long runs 10 of them when run alone from a cold
-// cache; 32768 rows 141 (floor 78), the sort 28, the sums 104, the joining 13.
+// cache; 32768 rows 141 (floor 78), the sort 30, the sums 100, the joining 14.
 // 128 rows of 256 into 1024 x 256: 12 us.  Sums by atomics instead of the sort
 // would neither repeat their bits nor allow one projection per token.
 #include <string.h>
@@ -343,6 +343,7 @@ __device__ void fill_rows(const RunSumParams& p, int first, int* absent) {
 // goes on to the right.  The rows a CTA reads are consecutive entries, so U of
 // them (and the table rows of the runs that end among them) are loaded at once.
 // Many CTAs matter more than many rows in flight in each: 64 registers a thread
+// (adding, 4 bytes of them spilled)
 // and two rows take 249 us where 120 registers and four rows took 259 (32768 rows
 // of 2048 into 131072 x 2048).
 template <int NV, int U, bool Add>

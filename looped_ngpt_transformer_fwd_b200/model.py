@@ -209,7 +209,8 @@ class Vocab:
         """(loss fp32 [n], d_logits [n, V]) of student logits z against a teacher's
         top logits (int32 / fp32 [n, k]; a negative token is an unused entry):
         loss[i] = w T^2 KL(softmax(teacher / T) || softmax(z / T)) and the gradient
-        of grad_scale * loss.sum() as `grad` (torch.float32, torch.bfloat16, or None
+        of grad_scale * loss.sum() (a token's entries add up in it; the loss is summed
+        over entries) as `grad` (torch.float32, torch.bfloat16, or None
         for the loss alone); through_scale carries it through the logit scale to
         the products emb_out . h.  An fp32 gradient may go to out = z."""
         dev, f32 = self.model.device, torch.float32
