@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) row_update_kernel(const 
 
 // ------------------------------------------------------------------ pipelined row update
 // The same update for many rows of one K slice without per-row loop counts
-// or a fused quantiser (bf16 prefill; 33.4 against 38.0 us per 4096-row
+// or a fused quantiser (bf16 prefill; 33.7 against 38.0 us per 4096-row
 // update of d_model 3072 on B200, cold L2): a persistent CTA streams its rows (r = blockIdx.x, + gridDim.x,
 // ...) through a ring of shared-memory stages that one producer lane fills
 // with bulk copies (y, h, and e when re-injecting: one d-float vector each),

@@ -13,7 +13,7 @@
 //
 // Bound: HBM where the table is written: 32768 rows of 2048 into 131072 x 2048
 // (tokens by frequency) 249 us, floor 212.  Adding to few rows is bound by the
-// chain of launches: 4096 rows into the same table 29 us (floor 12), the sort 8,
+// chain of launches: 4096 rows into the same table 30 us (floor 12), the sort 8,
 // the sums 20 and the joining of long runs 10 of them when run alone from a cold
 // cache; 32768 rows 141 (floor 78), the sort 30, the sums 100, the joining 14.
 // 128 rows of 256 into 1024 x 256: 12 us.  Sums by atomics instead of the sort
