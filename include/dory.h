@@ -326,8 +326,8 @@ DORY_API int dory_adjust_logits(dory_vocab* v, const float* logits, int n,
  * device): values [n, k] and tokens [n, k] (int32) in descending order, equal
  * values by ascending token (-0 equals +0; a NaN ranks below -inf), and lse [n]
  * = log sum_v exp(logits[v]) (-inf for a row of -inf, NaN for a row that holds
- * one), so that values - lse are log-probabilities.  What a teacher stores for dory_distill.  vocab at most
- * 2^20. */
+ * one), so that values - lse are log-probabilities.  What a teacher stores for
+ * dory_distill.  vocab at most 2^20. */
 #define DORY_MAX_TOP 256
 DORY_API int dory_top_logits(dory_vocab* v, const float* logits, int n, int k, float* values,
                              int32_t* tokens, float* lse, void* stream);
